@@ -284,7 +284,8 @@ int bsgemm_quantize_permute(const void* x, uint32_t x_dtype, const int32_t* topk
 
 /* q_fmt: a quantised output's element type and scale kind. Supported (K a multiple of 128):
  *   (E4M3, BLOCKWISE)  codes uint8[rows, K], scales float[rows, K/128]:
- *                      s = amax / 448 (1 if amax = 0), q = e4m3 of clamp(y / s, -448, 448)
+ *                      s = amax / 448 (1 if amax = 0, 2^-149 if it rounds to 0),
+ *                      q = e4m3 of clamp(y / s, -448, 448)
  *   (E4M3, MX)         codes uint8[rows, K], scales uint8[rows, K/32] (e8m0):
  *                      code = clamp(floor(log2 amax) - 8 + 127, 0, 254) (127 if amax = 0),
  *                      q = e4m3 of clamp(y 2^(127 - code), -448, 448)

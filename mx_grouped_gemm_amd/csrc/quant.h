@@ -172,7 +172,8 @@ __device__ __forceinline__ float clamp(float v, float most) { return __builtin_a
 // Quantises the lane's 8 values y (vector v of a matrix whose rows are whole blocks: codes and
 // scales of a row-major matrix are then indexed by v alone) and stores the codes; the block's
 // first lane stores its scale. All lanes of a block take part, or none.
-//   e4m3, fp32 scale of 128: s = amax / 448 (1 if amax is 0), codes of clamp(y / s), both fp32 divisions
+//   e4m3, fp32 scale of 128: s = amax / 448 (1 if amax is 0, 2^-149 if it rounds to 0), codes of clamp(y / s),
+//               both fp32 divisions
 //   e8m0 of 32: code = floor(log2 amax) - emax + 127 in [0, 254] (127 if amax is 0); y 2^(127 - code)
 //               is exact before the element's rounding and saturation
 //   nvfp4: s = e4m3 of min(amax / 6, 448) (1 if amax is 0, the least subnormal if it rounds to 0),
@@ -190,15 +191,18 @@ __device__ __forceinline__ void quantize_store(const float (&y)[8], long long v,
   const long long block = v / kLanes;
   float z[8];
   if constexpr (Q == kE4M3Block) {
-    const float s = amax == 0.f ? 1.0f : amax / 448.0f;
-    // |y / s| is at most 448 (1 + 2^-23), which rounds to 448: the clamp changes no code
+    float s = amax == 0.f ? 1.0f : amax / 448.0f;
     if (s >= 0x1p-100f && s <= 0x1p100f) {
+      // |y / s| is at most 448 (1 + 2^-23), which rounds to 448: a clamp would change no code
       const float r = 1.0f / s;
 #pragma unroll
       for (int k = 0; k < 8; k++) z[k] = divide(y[k], s, r);
     } else {
+      // a subnormal s has few bits, so that |y / s| may reach 671, past the largest code: without the clamp such
+      // quotients convert to NaN. The quotient of two infinities is NaN and stays it.
+      if (s == 0.f) s = 0x1p-149f;
 #pragma unroll
-      for (int k = 0; k < 8; k++) z[k] = y[k] / s;
+      for (int k = 0; k < 8; k++) z[k] = larger(-448.0f, __builtin_elementwise_minimum(y[k] / s, 448.0f));
     }
     if (first) ((float*)scales)[block] = s;
   } else if constexpr (Q == kE2M1NV) {

@@ -55,7 +55,7 @@ def quantize(y, elem, kind):
         scales = np.where(amax > 0, np.maximum(code, 1), 0x38).astype(np.uint8)
         z = b / decode_e4m3fn(scales).astype(np.float32)[..., None]
     else:
-        scales = np.where(amax > 0, amax / np.float32(448), np.float32(1)).astype(np.float32)
+        scales = np.where(amax > 0, np.maximum(amax / np.float32(448), np.float32(2.0 ** -149)), np.float32(1)).astype(np.float32)
         z = b / scales[..., None]
     z = np.clip(z, -most, most).reshape(R, K)
     return (encode_e4m3fn(z) if elem == "e4m3" else pack_nibbles(encode_e2m1(z))), scales

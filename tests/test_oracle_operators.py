@@ -92,3 +92,16 @@ def test_planted_mistakes_are_seen():
     q, s = oo.quantize(y, "e4m3", "blockwise")
     assert not np.array_equal(s[:, 0], s[:, 1])
     assert oo.encode_e2m1([2.5])[0] == 4 and oo.encode_e2m1([5.0])[0] == 6 and oo.encode_e2m1([0.25])[0] == 0
+
+
+def test_e4m3_blocks_of_the_smallest_values_have_finite_codes_and_scales():
+    """amax from 2^-149 on, where amax / 448 has few bits or rounds to 0: clamped codes, the scale never 0."""
+    n = np.arange(1, 9000, dtype=np.uint32)
+    y = np.zeros((n.size, 128), np.float32)
+    y[:, 0], y[:, 1] = n.view(np.float32), -n.view(np.float32)
+    q, s = oo.quantize(y, "e4m3", "blockwise")
+    v = formats.decode_e4m3fn(q)
+    assert np.all(np.isfinite(v)) and np.all(s > 0) and np.all(v[:, 2:] == 0) and np.array_equal(v[:, 0], -v[:, 1])
+    # the scale is amax / 448 to half of 2^-149, the code 448 of it or, cut, at most 224 steps of 2^-149 less
+    err = np.abs(v[:, 0] * s[:, 0].astype(np.float64) - y[:, 0])
+    assert np.all(err <= np.maximum(y[:, 0] * 2.0 ** -4, s[:, 0] * 2.0 ** -10) + 224 * 2.0 ** -149)
