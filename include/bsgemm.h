@@ -310,7 +310,8 @@ int bsgemm_quantize_permute(const void* x, uint32_t x_dtype, const int32_t* topk
  *           K .. 2 K - 1 are u: the output of a gate_up product). 16-byte aligned.
  *   rows    >= 0 (0 is a no-op); rows * K at most 2^35; K > 0 a multiple of 128, at most 2^30
  *   q       DEVICE codes (output), 16-byte aligned;  scales DEVICE (output), float-aligned for BLOCKWISE
- * y is formed in fp32 and quantised without rounding to x's type first.
+ * y is formed in fp32 and quantised without rounding to x's type first. SwiGLU: y is 0 for finite g < -87.3
+ * (where |g / (1 + exp(-g))| is below 1.1e-36) and finite u; an infinite g of either sign gives a NaN.
  * Errors: BSG_ERR_FMT (x_dtype, act, q_fmt), BSG_ERR_SHAPE, BSG_ERR_NULL, BSG_ERR_ALIGN,
  * BSG_ERR_DEVICE, BSG_ERR_LAUNCH.
  */

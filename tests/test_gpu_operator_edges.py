@@ -75,3 +75,30 @@ def test_smallest_products_of_swiglu_and_the_norm_to_e4m3():
         q, s, _, _ = bsg.bsgemm_rms_norm_quantize(h.cuda(), w.cuda(), E4M3_BLOCK, 1e-5)
         # (h rstd) w with rstd to (K / 64 + 20) U
         assert near(q, s, oo.rms_norm(h.numpy(), w.numpy(), 1e-5)[0])
+
+
+# --------------------------------------------------------------------------------------
+# gates that are not finite
+# --------------------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("elem,kind", oo.FORMS)
+def test_swiglu_shows_infinite_gates(elem, kind, dtype):
+    """A gate of -inf, +inf or NaN, with an ordinary other factor, gives its block a scale that is not finite: g / (1 +
+    exp(-g)) is NaN at -inf. Every other block is what it is without, gates far below 0 (0 there) among them."""
+    K, B = 384, oo.BLOCK[kind]
+    x = torch.randn(40, 2 * K, generator=torch.Generator().manual_seed(6)).to(dtype)
+    x[:, 5:K:97] = torch.finfo(dtype).min
+    x[:, 6:K:89] = -88.0
+    fmt = bsg.make_quant(elem, kind)
+    q0, s0 = (t.cpu().numpy() for t in bsg.bsgemm_quantize(x.cuda(), fmt, act="swiglu"))
+    bad = np.zeros((40, K // B), bool)
+    for r in range(1, 40):
+        at = (r * 61) % K
+        x[r, at] = (-float("inf"), float("inf"), float("nan"))[r % 3]
+        bad[r, at // B] = True
+    q, s = (t.cpu().numpy() for t in bsg.bsgemm_quantize(x.cuda(), fmt, act="swiglu"))
+    lost = {"blockwise": lambda v: ~np.isfinite(v), "mx": lambda v: v == 255, "nv": lambda v: v == 0x7F}[kind]
+    assert not lost(s0).any() and np.array_equal(lost(s), bad)
+    assert np.array_equal(s[~bad], s0[~bad])
+    q, q0 = (t.reshape(40, K // B, -1) for t in (q, q0))
+    assert np.array_equal(q[~bad], q0[~bad])
