@@ -202,11 +202,14 @@ extern "C" int bsgemm_grouped_few_rows(const void* A, const void* a_scales, cons
   const bool dense = !expert_ids && !tile_offsets;
   const int32_t tiles = dense ? (int32_t)(((long long)M + 127) / 128) : num_tiles;
   if ((long long)tiles * (N / 32) > (1 << 21)) return BSG_ERR_SHAPE;
-  if ((!dense && (!expert_ids || !tile_offsets)) || !A || !a_scales || !B || !b_scales || !C) return BSG_ERR_NULL;
+  // an empty tensor's pointer is NULL: a call with nothing to do takes it
+  const bool none = M == 0 || tiles == 0;
+  if ((!dense && ((num_tiles > 0 && !expert_ids) || !tile_offsets)) || (!none && (!A || !a_scales || !B || !b_scales || !C)))
+    return BSG_ERR_NULL;
   if (!aligned(A, 16) || !aligned(B, 16) || !aligned(C, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
       !aligned(expert_ids, 4) || !aligned(tile_offsets, 4))
     return BSG_ERR_ALIGN;
-  if (M == 0 || tiles == 0) return BSG_OK;
+  if (none) return BSG_OK;
   bsg::GemmArgs args{};
   if (int st = check_device(&args.num_cus)) return st;
   args.A = A;

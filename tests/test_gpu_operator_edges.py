@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import mx_grouped_gemm_amd as bsg
+from examples import moe_block
 from oracle import formats, operators as oo
 from tests.parity import say
 
@@ -102,3 +103,16 @@ def test_swiglu_shows_infinite_gates(elem, kind, dtype):
     assert np.array_equal(s[~bad], s0[~bad])
     q, q0 = (t.reshape(40, K // B, -1) for t in (q, q0))
     assert np.array_equal(q[~bad], q0[~bad])
+
+
+# --------------------------------------------------------------------------------------
+# no rows
+# --------------------------------------------------------------------------------------
+def test_a_block_without_tokens():
+    """Every operator with empty tensors, forward and gradient: a rank that got no tokens."""
+    block = moe_block.random_block(4, 256, 128, 2)
+    x = torch.empty(0, 256, dtype=torch.bfloat16, device="cuda")
+    out, saved = moe_block.forward(block, x, x)
+    assert out.shape == (0, 256) and not saved["counts"].any() and not saved["offsets"].any()
+    dx, dnorm, drouter = moe_block.backward(block, saved, out, x)
+    assert dx.shape == (0, 256) and not dnorm.any() and not drouter.any()

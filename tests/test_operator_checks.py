@@ -186,3 +186,13 @@ def test_binding_checks(fn, good, bad):
     for over in bad:
         with pytest.raises(ValueError):
             fn(**{**good, **over})
+
+
+def test_grouped_few_rows_without_rows_takes_the_null_pointers_of_empty_tensors():
+    assert torch.empty(0, 128).data_ptr() == 0
+    base = dict(A=None, sa=None, B=P, sb=P, ei=P, to=P, T=2, C=None, M=0, N=256, K=640, E=2,
+                fmt=bsg.make_fmt("e2m1", "e2m1", "mx", "bf16"), stream=None)
+    for want, over in [(OK, {}), (OK, dict(ei=None, to=None)), (OK, dict(T=0, ei=None)), (OK, dict(T=0, ei=None, M=4)),
+                       (OK, dict(B=None, sb=None)), (NULL, dict(ei=None)), (NULL, dict(to=None)), (NULL, dict(M=4)),
+                       (NULL, dict(T=0, to=None)), (SHAPE, dict(N=100)), (ALIGN, dict(B=P4))]:
+        assert call("bsgemm_grouped_few_rows", base, **over) == want, (over, want)
