@@ -31,7 +31,7 @@ uintptr_t scale_align(int quant) { return quant == 0 ? 4 : 1; }
 
 constexpr int32_t kMaxNormK = 32768;         // a row is held in one workgroup's registers
 constexpr int32_t kMaxNormRows = (1 << 22) - 1;   // a workgroup of up to 1024 threads each
-constexpr int32_t kMaxPicks = 1 << 24;       // of a sort: 4096 chunks
+constexpr int32_t kMaxPicks = 1 << 24;       // of a sort: 4096 chunks, 8192 above 2048 experts
 constexpr int32_t kMaxRowsK = 1 << 22;       // K of the few-row product: its 256-row buffers stay under 2 GiB
 constexpr long long kMaxElems = 1LL << 35;   // rows x K of the quantiser, twice SwiGLU's: grids stay within 32 bits
 

@@ -1,5 +1,5 @@
 // Stable sort of top-k picks by expert (gfx950): per-expert counts, group offsets, the M-tile map
-// and the row of every pick, in one or two launches.
+// and the row of every pick, in one to three launches.
 //
 //   counts[e]         picks i with ids[i] = e (ids outside [0, E) are dropped)
 //   expert_offsets    exclusive sums of the groups' rows (padded: whole 128-row tiles)
@@ -10,8 +10,10 @@
 // it. In a wave 64 picks are matched against each other by ballots over the bits of
 // their ids, which gives each pick its place among equals without atomics, so the order is the
 // picks' own on every call. With one chunk everything happens in one launch (a decode batch); with
-// more, a first launch writes every chunk's histogram, and each workgroup of the second sums the
-// chunks before its own. What bounds it is the latency of these steps, not their bytes.
+// more, a first launch writes every chunk's histogram, and each workgroup of the last sums the
+// chunks before its own. Where that is much (see kMostCounts), a launch in between turns the histograms into
+// these sums, so that the work grows with the picks, not with their square. What bounds it is the latency of
+// these steps, not their bytes.
 #include "ops_launch.h"
 #include "quant.h"
 
@@ -29,6 +31,14 @@ int chunks_of(int n, int E) {
   const int chunk = waves_for(E) * kSegment;
   return n <= chunk ? 1 : (n + chunk - 1) / chunk;
 }
+// Most counts (chunks x experts) that every workgroup of the last launch sums itself. Measured (us a call in a
+// graph; itself, with the launch in between):
+//     4096 counts, 256 experts   18.3   19.7        16384 counts, 256 experts   26.4   20.1
+//     8192 counts,   8 experts   31.0   34.7        32768 counts,  32 experts   61.3   39.3
+//     8192 counts,  32 experts   19.1   18.2       262144 counts, 256 experts    304   47.4
+//     8192 counts, 512 experts   22.4   20.8      2097152 counts, 4096 experts  5475   83.9
+constexpr int kMostCounts = 8192;
+
 // place[waves][E], row_start[E + 1], tile_start[E + 1], total[E], before[E]
 constexpr size_t lds_bytes(int waves, int E) { return ((size_t)waves * E + 2 * (E + 1) + 2 * E) * sizeof(int); }
 static_assert(lds_bytes(8, 2048) + 64 <= 160 * 1024 && lds_bytes(4, 4096) + 64 <= 160 * 1024, "LDS");
@@ -87,10 +97,42 @@ __global__ __launch_bounds__(kWaves* kWave) void route_chunk_counts_kernel(const
   for (int e = threadIdx.x; e < E; e += kThreads) chunk_counts[(long long)blockIdx.x * E + e] = hist[e];
 }
 
+// Each chunk's row of chunk_counts becomes the picks of every expert in the chunks before it, and the row behind
+// them the totals: 64 experts per workgroup, a 16th of the chunks per wave, 16 loads on their way at once.
+__global__ __launch_bounds__(1024) void route_chunk_starts_kernel(int32_t* chunk_counts, int chunks, int E) {
+  __shared__ int part[16][kWave];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.x * kWave + lane;
+  const int per = (chunks + 15) / 16, first = wave * per, last = min(first + per, chunks);
+  auto load = [&](int c0, int (&v)[16]) {
+#pragma unroll
+    for (int i = 0; i < 16; i++) v[i] = e < E && c0 + i < last ? chunk_counts[(long long)(c0 + i) * E + e] : 0;
+  };
+  int sum = 0, v[16];
+  for (int c0 = first; c0 < last; c0 += 16) {
+    load(c0, v);
+#pragma unroll
+    for (int i = 0; i < 16; i++) sum += v[i];
+  }
+  part[wave][lane] = sum;
+  __syncthreads();
+  int next = 0;
+  for (int w = 0; w < wave; w++) next += part[w][lane];
+  for (int c0 = first; c0 < last; c0 += 16) {
+    load(c0, v);
+#pragma unroll
+    for (int i = 0; i < 16; i++) {
+      if (e < E && c0 + i < last) chunk_counts[(long long)(c0 + i) * E + e] = next;
+      next += v[i];
+    }
+  }
+  if (wave == 15 && e < E) chunk_counts[(long long)chunks * E + e] = next;
+}
+
 // segment: consecutive picks per wave, a multiple of 64 (with one chunk, what spreads it over all waves).
+// starts: chunk_counts are the sums of route_chunk_starts_kernel.
 template <int kWaves>
 __global__ __launch_bounds__(kWaves* kWave) void route_sort_kernel(
-    const int32_t* __restrict__ ids, int n, int segment, int E, int bits, int T, int padded, int M,
+    const int32_t* __restrict__ ids, int n, int segment, int E, int bits, int T, int padded, int M, int starts,
     const int32_t* __restrict__ chunk_counts, int32_t* __restrict__ counts, int32_t* __restrict__ expert_offsets,
     int32_t* __restrict__ tile_offsets, int32_t* __restrict__ expert_ids, int32_t* __restrict__ dest) {
   constexpr int kThreads = kWaves * kWave;
@@ -107,14 +149,21 @@ __global__ __launch_bounds__(kWaves* kWave) void route_sort_kernel(
   int id[kSteps];
   load_picks(ids, n, begin, steps, E, id);
   for (int i = tid; i < kWaves * E; i += kThreads) place[i] = 0;
-  for (int i = tid; i < 2 * E; i += kThreads) total_of[i] = 0;
+  if (starts) {
+    for (int e = tid; e < E; e += kThreads) {
+      total_of[e] = chunk_counts[(long long)chunks * E + e];
+      before_of[e] = chunk_counts[(long long)chunk * E + e];
+    }
+  } else {
+    for (int i = tid; i < 2 * E; i += kThreads) total_of[i] = 0;
+  }
   __syncthreads();
   int* mine = place + wave * E;                    // next row of this wave's picks of an expert
   histogram(id, steps, bits, mine);
-  if (chunks > 1) {
-    const long long all = (long long)chunks * E, earlier = (long long)chunk * E;
-    for (long long i = tid; i < all; i += kThreads) {
-      const int v = chunk_counts[i], e = (int)(i % E);
+  if (chunks > 1 && !starts) {
+    const int all = chunks * E, earlier = chunk * E;      // all: at most kMostCounts
+    for (int i = tid; i < all; i += kThreads) {
+      const int v = chunk_counts[i], e = i % E;
       if (v) {
         atomicAdd(&total_of[e], v);
         if (i < earlier) atomicAdd(&before_of[e], v);
@@ -220,14 +269,19 @@ hipError_t launch(const int32_t* ids, int n, int E, int T, int padded, int M, in
   int bits = 0;
   while ((1 << bits) < E) bits++;
   const int chunks = chunks_of(n, E);
+  const bool starts = chunks > 1 && (long long)chunks * E > kMostCounts;
   const int segment = chunks > 1 ? kSegment : max(1, (n + kWaves * kWave - 1) / (kWaves * kWave)) * kWave;
   const dim3 grid(chunks), block(kWaves * kWave);
   if (chunks > 1) {
     hipLaunchKernelGGL(route_chunk_counts_kernel<kWaves>, grid, block, E * sizeof(int), s, ids, n, E, bits, workspace);
     if (hipError_t e = hipGetLastError()) return e;
   }
+  if (starts) {
+    hipLaunchKernelGGL(route_chunk_starts_kernel, dim3((E + kWave - 1) / kWave), dim3(1024), 0, s, workspace, chunks, E);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
   hipLaunchKernelGGL(route_sort_kernel<kWaves>, grid, block, lds_bytes(kWaves, E), s, ids, n, segment, E, bits, T, padded,
-                     M, workspace, counts, expert_offsets, tile_offsets, expert_ids, dest);
+                     M, starts ? 1 : 0, workspace, counts, expert_offsets, tile_offsets, expert_ids, dest);
   return hipGetLastError();
 }
 
@@ -235,7 +289,7 @@ hipError_t launch(const int32_t* ids, int n, int E, int T, int padded, int M, in
 
 size_t route_sort_workspace_bytes(int n, int E) {
   const int chunks = chunks_of(n, E);
-  return chunks > 1 ? (size_t)chunks * E * sizeof(int32_t) : 0;
+  return chunks > 1 ? ((size_t)chunks + 1) * E * sizeof(int32_t) : 0;      // the histograms and their totals
 }
 
 hipError_t launch_route_sort(const int32_t* ids, int n, int E, int T, int padded, int M, int32_t* counts,

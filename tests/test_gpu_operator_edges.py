@@ -8,7 +8,7 @@ import torch
 
 import mx_grouped_gemm_amd as bsg
 from examples import moe_block
-from oracle import formats, operators as oo
+from oracle import formats, gemm as og, operators as oo, permute as op
 from tests.parity import say
 
 pytestmark = pytest.mark.gpu
@@ -190,3 +190,58 @@ def test_few_rows_product_beside_a_large_one(fa, fb):
     err = np.abs(C.cpu().double().numpy() - a @ b.T)
     say(f"[few rows] {fa}x{fb} beside large products: {err.max() / (a @ b.T).max():.2e} of sum |a||b|")
     assert np.all(err <= product_bound(a, b, True))
+
+
+# --------------------------------------------------------------------------------------
+# sorts of many picks
+# --------------------------------------------------------------------------------------
+@pytest.mark.parametrize("padded", [True, False])
+@pytest.mark.parametrize("n,E", [(131072, 65), (4096 * 17 + 1, 500), (4096 * 16, 513), (2048 * 5 + 77, 2049), (2048 * 300, 28),
+                                 (300001, 256), (2048 * 33 - 1, 4096)])
+def test_route_sort_of_many_chunks(n, E, padded):
+    """About the number of counts at which the chunks' sums take a launch of their own, and past it."""
+    rng = np.random.default_rng(n)
+    ids = rng.choice(E + 3, n, p=rng.dirichlet(np.full(E + 3, 0.5))).astype(np.int32) - 1      # -1, E and E + 1 are strays
+    counts = op.route_counts(ids[None], E)
+    T = -(-n // 128) + E
+    eor, tor, eir = og.tile_map(counts, T, padded)
+    dest, c, eo, to, ei = bsg.bsgemm_route_sort(torch.from_numpy(ids).cuda(), E, T, 128 * T, padded=padded)
+    assert np.array_equal(c.cpu().numpy(), counts) and np.array_equal(eo.cpu().numpy(), eor)
+    assert np.array_equal(to.cpu().numpy(), tor) and np.array_equal(ei.cpu().numpy(), eir)
+    assert np.array_equal(dest.cpu().numpy(), op.permute_dest(ids[None], eor, 128 * T)[0])
+
+
+@pytest.mark.parametrize("n,E", [(1 << 24, 4096), ((1 << 24) - 5, 2048), (1 << 24, 3)])
+def test_route_sort_of_the_most_picks(n, E):
+    """The largest sorts there are, against torch's stable sort."""
+    ids = torch.randint(0, E, (n,), dtype=torch.int32, device="cuda", generator=torch.Generator("cuda").manual_seed(E))
+    T = -(-n // 128) + E
+    dest, c, eo, _, _ = bsg.bsgemm_route_sort(ids, E, T, n, padded=False)
+    order = torch.sort(ids, stable=True).indices
+    want = torch.empty_like(order)
+    want[order] = torch.arange(n, device="cuda")
+    assert torch.equal(dest.long(), want)
+    assert torch.equal(c.long(), torch.bincount(ids, minlength=E)) and torch.equal(eo[1:].long(), torch.cumsum(c, 0))
+
+
+def test_route_sort_work_grows_with_the_picks():
+    """8 times the picks take at most 16 times as long (every workgroup summing all histograms: 32 times)."""
+    E = 4096
+
+    def best(n):
+        ids = torch.randint(0, E, (n,), dtype=torch.int32, device="cuda")
+        ws = torch.empty(bsg.bsgemm_route_sort_workspace_size(n, E), dtype=torch.uint8, device="cuda")
+        bufs = bsg.bsgemm_route_sort(ids, E, 0, n, padded=False, workspace=ws)
+        times = []
+        for _ in range(5):
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            bsg.bsgemm_route_sort(ids, E, 0, n, padded=False, dest=bufs[0], counts=bufs[1], workspace=ws)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(begin.elapsed_time(end))
+        return min(times)
+
+    short, long = best(1 << 18), best(1 << 21)
+    say(f"[sort] 4096 experts: 2^18 picks {1e3 * short:.0f} us, 2^21 {1e3 * long:.0f} us")
+    assert long <= 16 * short
