@@ -91,16 +91,16 @@ constexpr int kGroup = 8;                    // steps whose scales are staged at
 constexpr int kGroupChunks = kGroup / kWideSteps;
 
 // LDS of a workgroup. Two stages of A: a chunk of the tile's rows in 16-byte slots, slot c of row r at
-// place c ^ (r % 16) of its row (c ^ (r / 2 % 8) in rows of 8 slots), which spreads one slot of a
-// fragment's 16 rows over all banks. Two stages of scales: a group of the tile's rows, then of every
-// wave's columns, 32 bytes each.
+// place c ^ (r % 16) of its row, which spreads one slot of a fragment's 16 rows over all banks. Two
+// stages of scales: a group of the tile's rows, then of every wave's columns, 32 bytes each.
 template <int FA, int W> struct WideLds {
   static constexpr int kRowBytes = kWideSteps * Elem<FA>::kStepBytes, kSlots = kRowBytes / 16;
   static constexpr int kStage = kTileRows * kRowBytes;
   static constexpr int kScaleRow = 4 * kGroup, kScales = 2 * kStage, kScaleStage = (kTileRows + W * kWaveCols) * kScaleRow;
   static constexpr int kBytes = kScales + 2 * kScaleStage;
   static_assert(kBytes <= 160 * 1024, "LDS");
-  static __device__ __forceinline__ int place(int r, int c) { return c ^ (kSlots == 8 ? (r >> 1) & 7 : r & 15); }
+  static_assert(kSlots % 16 == 0, "slots are exchanged within 16");
+  static __device__ __forceinline__ int place(int r, int c) { return c ^ (r & 15); }
 };
 
 // Copies chunk `ch` of 16 NF rows, shared by the waves: 1 KiB an instruction.
@@ -350,14 +350,12 @@ __global__ __launch_bounds__(kSplitWaves* kWave) void mx_few_rows_split_kernel(G
   }
 }
 
-// A grid's threads are counted in 32 bits.
-bool fits(long long blocks, int waves) { return blocks * waves * kWave <= 0xffffffffLL; }
+static_assert(2 * kMaxFewRowsCols * kSplitWaves * kWave <= kMaxThreads, "the split schedule's grid, the larger one");
 
 template <int FA, int FB, int OUT, int W>
 hipError_t launch_wide(const GemmArgs& a, int n_blocks, hipStream_t s) {
-  const long long blocks = (long long)a.num_tiles * n_blocks;
-  if (!fits(blocks, W)) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((mx_few_rows_wide_kernel<FA, FB, OUT, W>), dim3((unsigned)blocks), dim3(W * kWave), 0, s, a, n_blocks);
+  hipLaunchKernelGGL((mx_few_rows_wide_kernel<FA, FB, OUT, W>), dim3((unsigned)(a.num_tiles * n_blocks)), dim3(W * kWave), 0, s,
+                     a, n_blocks);
   return hipGetLastError();
 }
 
@@ -388,7 +386,6 @@ hipError_t launch(const GemmArgs& a, hipStream_t s) {
   if (blocks(2) > a.num_cus) return launch_wide<FA, FB, OUT, 4>(a, n_blocks(4), s);
   if (2 * blocks(2) >= a.num_cus) return launch_wide<FA, FB, OUT, 2>(a, n_blocks(2), s);
   const int split = a.N / kSplitCols;
-  if (!fits((long long)a.num_tiles * split, kSplitWaves)) return hipErrorInvalidValue;
   hipLaunchKernelGGL((mx_few_rows_split_kernel<FA, FB, OUT>), dim3((unsigned)(a.num_tiles * split)),
                      dim3(kSplitWaves * kWave), 0, s, a, split);
   return hipGetLastError();

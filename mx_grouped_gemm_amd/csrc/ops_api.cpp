@@ -33,7 +33,6 @@ constexpr int32_t kMaxNormK = 32768;         // a row is held in one workgroup's
 constexpr int32_t kMaxNormRows = (1 << 22) - 1;   // a workgroup of up to 1024 threads each
 constexpr int32_t kMaxPicks = 1 << 24;       // of a sort: 4096 chunks, 8192 above 2048 experts
 constexpr int32_t kMaxRowsK = 1 << 22;       // K of the few-row product: its 256-row buffers stay under 2 GiB
-constexpr long long kMaxElems = 1LL << 35;   // rows x K of the quantiser, twice SwiGLU's: grids stay within 32 bits
 
 int status(hipError_t e) { return e == hipSuccess ? BSG_OK : BSG_ERR_LAUNCH; }
 
@@ -41,8 +40,8 @@ bool picks_ok(int32_t tokens, int32_t top_k) {
   return tokens >= 0 && top_k >= 1 && (long long)tokens * top_k <= INT32_MAX;
 }
 
-// Waves of the row moves, 64 vectors of a row each: their grids' threads are counted in 32 bits.
-bool waves_ok(int32_t tokens, int32_t row_vecs) { return (long long)tokens * ((row_vecs + 63LL) / 64) <= (1LL << 25); }
+// Waves of the row moves, 64 vectors of a row each.
+bool waves_ok(int32_t tokens, int32_t row_vecs) { return (long long)tokens * ((row_vecs + 63LL) / 64) <= bsg::kMaxMoveWaves; }
 
 }  // namespace
 
@@ -50,7 +49,7 @@ extern "C" int bsgemm_quantize(const void* x, uint32_t x_dtype, uint32_t act, in
                                void* q, void* scales, void* stream) {
   const int quant = quant_kind(q_fmt);
   if (!row_type(x_dtype) || quant < 0 || (act != BSG_ACT_NONE && act != BSG_ACT_SWIGLU)) return BSG_ERR_FMT;
-  if (rows < 0 || K <= 0 || K % 128 || K > (1 << 30) || (long long)rows * K > kMaxElems) return BSG_ERR_SHAPE;
+  if (rows < 0 || K <= 0 || K % 128 || K > (1 << 30) || (long long)rows * K > bsg::kMaxElems) return BSG_ERR_SHAPE;
   if (rows > 0 && (!x || !q || !scales)) return BSG_ERR_NULL;
   if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scales, scale_align(quant))) return BSG_ERR_ALIGN;
   if (rows == 0) return BSG_OK;
@@ -62,7 +61,7 @@ extern "C" int bsgemm_quantize(const void* x, uint32_t x_dtype, uint32_t act, in
 extern "C" int bsgemm_swiglu_backward(const void* dy, const void* x, uint32_t dtype, int32_t rows, int32_t K, void* dx,
                                       void* stream) {
   if (!row_type(dtype)) return BSG_ERR_FMT;
-  if (rows < 0 || K <= 0 || K % 8 || K > (1 << 30) || (long long)rows * K > kMaxElems / 2) return BSG_ERR_SHAPE;
+  if (rows < 0 || K <= 0 || K % 8 || K > (1 << 30) || (long long)rows * K > bsg::kMaxElems / 2) return BSG_ERR_SHAPE;
   if (rows > 0 && (!dy || !x || !dx)) return BSG_ERR_NULL;
   if (!aligned(dy, 16) || !aligned(x, 16) || !aligned(dx, 16)) return BSG_ERR_ALIGN;
   if (rows == 0) return BSG_OK;
@@ -115,7 +114,7 @@ extern "C" int bsgemm_rms_norm_backward(const void* dy, const void* h, const voi
 }
 
 extern "C" int bsgemm_route_sort_workspace_size(int32_t num_picks, int32_t num_experts, size_t* bytes) {
-  if (num_picks < 0 || num_picks > kMaxPicks || num_experts < 1 || num_experts > 4096) return BSG_ERR_SHAPE;
+  if (num_picks < 0 || num_picks > kMaxPicks || num_experts < 1 || num_experts > bsg::kMaxExperts) return BSG_ERR_SHAPE;
   if (!bytes) return BSG_ERR_NULL;
   *bytes = bsg::route_sort_workspace_bytes(num_picks, num_experts);
   return BSG_OK;
@@ -125,7 +124,7 @@ extern "C" int bsgemm_route_sort(const int32_t* topk_ids, int32_t num_picks, int
                                  int32_t padded, int32_t M, int32_t* counts, int32_t* expert_offsets,
                                  int32_t* tile_offsets, int32_t* expert_ids, int32_t* dest, void* workspace,
                                  size_t workspace_bytes, void* stream) {
-  if (num_picks < 0 || num_picks > kMaxPicks || num_experts < 1 || num_experts > 4096 || num_tiles < 0 ||
+  if (num_picks < 0 || num_picks > kMaxPicks || num_experts < 1 || num_experts > bsg::kMaxExperts || num_tiles < 0 ||
       num_tiles == INT32_MAX || M < 0)
     return BSG_ERR_SHAPE;
   const size_t need = bsg::route_sort_workspace_bytes(num_picks, num_experts);
@@ -145,7 +144,7 @@ extern "C" int bsgemm_route_sort(const int32_t* topk_ids, int32_t num_picks, int
 extern "C" int bsgemm_permute_rows(const void* x, int32_t row_bytes, const int32_t* dest, int32_t tokens,
                                    int32_t top_k, const int32_t* counts, const int32_t* expert_offsets,
                                    int32_t num_experts, int32_t M, void* out, void* stream) {
-  if (!picks_ok(tokens, top_k) || row_bytes <= 0 || row_bytes % 4 || num_experts < 1 || num_experts > 4096 || M < 0 ||
+  if (!picks_ok(tokens, top_k) || row_bytes <= 0 || row_bytes % 4 || num_experts < 1 || num_experts > bsg::kMaxExperts || M < 0 ||
       !waves_ok(tokens, row_bytes / 4))
     return BSG_ERR_SHAPE;
   if (!counts || !expert_offsets || (tokens > 0 && (!x || !dest)) || (M > 0 && !out)) return BSG_ERR_NULL;
@@ -174,8 +173,8 @@ extern "C" int bsgemm_combine_backward(const void* dout, const void* y, uint32_t
                                        const int32_t* counts, const int32_t* expert_offsets, int32_t num_experts,
                                        int32_t M, void* dy, float* dweights, void* stream) {
   if (!row_type(dtype)) return BSG_ERR_FMT;
-  if (!picks_ok(tokens, top_k) || K <= 0 || K % 8 || K > (INT32_MAX / 4) || num_experts < 1 || num_experts > 4096 ||
-      M < 0 || tokens > (1 << 23))
+  if (!picks_ok(tokens, top_k) || K <= 0 || K % 8 || K > (INT32_MAX / 4) || num_experts < 1 || num_experts > bsg::kMaxExperts ||
+      M < 0 || tokens > bsg::kMaxGradTokens)
     return BSG_ERR_SHAPE;
   if (!counts || !expert_offsets || (tokens > 0 && (!dout || !dest || !weights || !dweights)) ||
       (M > 0 && (!y || !dy)))
@@ -201,7 +200,7 @@ extern "C" int bsgemm_grouped_few_rows(const void* A, const void* a_scales, cons
     return BSG_ERR_SHAPE;
   const bool dense = !expert_ids && !tile_offsets;
   const int32_t tiles = dense ? (int32_t)(((long long)M + 127) / 128) : num_tiles;
-  if ((long long)tiles * (N / 32) > (1 << 21)) return BSG_ERR_SHAPE;
+  if ((long long)tiles * (N / 32) > bsg::kMaxFewRowsCols) return BSG_ERR_SHAPE;
   // an empty tensor's pointer is NULL: a call with nothing to do takes it
   const bool none = M == 0 || tiles == 0;
   if ((!dense && ((num_tiles > 0 && !expert_ids) || !tile_offsets)) || (!none && (!A || !a_scales || !B || !b_scales || !C)))

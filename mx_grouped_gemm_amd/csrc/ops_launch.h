@@ -9,6 +9,15 @@
 
 namespace bsg {
 
+// Size limits that the entry points check, so that every grid's threads fit the 32 bits they are counted in: each
+// launcher has a static_assert of what it makes of them.
+constexpr long long kMaxThreads = 0xffffffffLL;
+constexpr long long kMaxElems = 1LL << 35;     // rows x K of the quantiser, twice those of SwiGLU's gradient
+constexpr long long kMaxMoveWaves = 1LL << 25; // of the row moves: tokens x 64 vectors of a row
+constexpr long long kMaxGradTokens = 1LL << 23;       // of the weighted sum's gradient
+constexpr int kMaxExperts = 4096;
+constexpr long long kMaxFewRowsCols = 1LL << 21;      // of the few-row product: tiles x 32 columns
+
 // Row types (`dtype`) are the BSG_OUT_* codes: 1 f32, 2 bf16, 3 f16. Quantised forms (`quant`) are the
 // QuantKind codes of quant.h.
 

@@ -15,6 +15,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 2;               // vectors per thread
+static_assert(kMaxElems / 8 / kPer + kThreads <= kMaxThreads && kMaxElems / 2 / 8 + kThreads <= kMaxThreads,
+              "grids of the quantiser and of SwiGLU's gradient");
 
 // exp(-c) for c <= 100 as 2^t 2^r: t, the rounded product -c log2(e), by the instruction for 2^x, r what its
 // rounding left (2^r = 1 + r ln 2 to fp32; without r the error grows by |c| 2^-24, and 1.7 times as many codes
@@ -121,7 +123,6 @@ hipError_t launch(const void* x, int rows, int K, int quant, uint8_t* q, void* s
   const int row_vecs = K / 8;
   const long long vecs = (long long)rows * row_vecs;
   const long long blocks = (vecs + kThreads * kPer - 1) / (kThreads * kPer);
-  if (blocks > 0x7fffffffLL) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(kThreads);
   switch (quant) {
     case kE4M3Block: hipLaunchKernelGGL((quantize_rows_kernel<T, ACT, kE4M3Block>), grid, block, 0, s, x, vecs, row_vecs, q, scales); break;

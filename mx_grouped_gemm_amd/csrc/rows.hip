@@ -205,8 +205,9 @@ __global__ __launch_bounds__(kThreads) void combine_backward_kernel(
 // Workgroups per expert for the padding rows: about 256 in all.
 int padding_parts(int E) { return E >= 256 ? 1 : 256 / E; }
 
-// A grid's threads are counted in 32 bits.
-bool fits(long long blocks) { return blocks * kThreads <= 0xffffffffLL; }
+static_assert(kMaxMoveWaves * kWave + (kMaxExperts + 1) * kThreads <= kMaxThreads &&
+                  (kMaxGradTokens + kMaxExperts) * kThreads <= kMaxThreads,
+              "grids with at most kMaxExperts workgroups for padding rows");
 
 // Waves of a row, and workgroups of the row moves.
 int pieces(int row_vecs) { return (row_vecs + kWave - 1) / kWave; }
@@ -240,7 +241,6 @@ hipError_t launch_permute(const void* x, int row_vecs, const int32_t* dest, int 
                           const int32_t* expert_offsets, int E, int M, void* out, hipStream_t s) {
   const long long move = move_blocks_of(tokens, row_vecs);
   const int parts = padding_parts(E);
-  if (!fits(move + (long long)E * parts)) return hipErrorInvalidValue;
   return with_picks(top_k, [&](auto g) {
     hipLaunchKernelGGL((permute_rows_kernel<V, decltype(g)::value>), dim3((unsigned)(move + E * parts)), dim3(kThreads), 0,
                        s, (const V*)x, dest, tokens, top_k, row_vecs, pieces(row_vecs), counts, expert_offsets, parts,
@@ -254,7 +254,6 @@ hipError_t launch_combine(const void* y, const int32_t* dest, const float* weigh
                           void* out, hipStream_t s) {
   const int V = K / 8;
   const long long blocks = move_blocks_of(tokens, V);
-  if (!fits(blocks)) return hipErrorInvalidValue;
   return with_picks(top_k, [&](auto g) {
     hipLaunchKernelGGL((combine_rows_kernel<T, kWeighted, decltype(g)::value>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
                        y, dest, weights, tokens, top_k, V, pieces(V), M, out);
@@ -269,7 +268,6 @@ hipError_t launch_combine_bwd(const void* dout, const void* y, const int32_t* de
   const int parts = padding_parts(E);
   const bool narrow = K / 8 <= kWave;      // a vector per lane
   const long long blocks = (narrow ? (tokens + 3LL) / 4 : (long long)tokens) + (long long)E * parts;
-  if (!fits(blocks)) return hipErrorInvalidValue;
   return with_picks(top_k, [&](auto g) {
     constexpr int G = decltype(g)::value;
     hipLaunchKernelGGL((narrow ? combine_backward_kernel<T, G, 1> : combine_backward_kernel<T, G, kThreads / kWave>),
