@@ -6,6 +6,10 @@ sizes of the call, since the C ABI sees bare pointers: ValueError where its shap
 layout is not what the call needs (``check_*`` make the same checks without a call, on any device).
 Sizes the library itself rejects come back as :class:`BsgemmError`. Outputs that are not given are
 allocated on the stream the call runs on.
+
+Results have no autograd history, also where an input requires a gradient: the gradients are calls of
+their own (``*_backward``; that of ``bsgemm_permute_rows`` is ``bsgemm_combine_rows`` without weights), which
+a ``torch.autograd.Function`` or a hand-written backward pass makes.
 """
 
 import ctypes
@@ -187,7 +191,8 @@ def check_quantize_args(x, q_fmt, act, q=None, scales=None):
 
 def bsgemm_quantize(x, q_fmt, act="none", q=None, scales=None, stream=None):
     """Rows ``x`` [rows, K], or the SwiGLU of ``x`` [rows, 2 K], in the quantised form ``q_fmt``
-    (:func:`make_quant`). Returns (codes uint8, scales)."""
+    (:func:`make_quant`). Returns (codes uint8, scales), detached from autograd: SwiGLU's gradient is
+    ``bsgemm_swiglu_backward``."""
     here = _device()
     code, rows, K, layout, px, pq, ps = _quantize_args(here, x, q_fmt, act, q, scales)
     if q is None:
@@ -250,7 +255,7 @@ def bsgemm_rms_norm_quantize(x, weight, q_fmt, eps=1e-6, residual=None, residual
                              scales=None, stream=None):
     """RMS norm of ``x + residual`` (``x`` without one) in the quantised form ``q_fmt``. Returns
     (codes, scales, residual_out, rstd); residual_out, the rounded sum, is None without a residual
-    and may be given as ``residual`` itself."""
+    and may be given as ``residual`` itself. Detached from autograd: the gradient is ``bsgemm_rms_norm_backward``."""
     here = _device()
     code, rows, K, layout, px, pw, pr, po, pd, pq, ps = _norm_args(here, x, weight, q_fmt, residual, residual_out, rstd,
                                                                    q, scales)
@@ -401,7 +406,8 @@ def check_permute_rows_args(x, dest, counts, expert_offsets, M, out=None):
 def bsgemm_permute_rows(x, dest, counts, expert_offsets, M, out=None, stream=None):
     """Rows of ``x`` [tokens, K] (any element type, rows of whole 4-byte words) at the rows of their picks
     in ``out`` [M, K]; padding rows of the groups are zero, other rows untouched. Returns ``out``
-    (zeros outside the groups if it is allocated here)."""
+    (zeros outside the groups if it is allocated here), detached from autograd: the gradient is
+    ``bsgemm_combine_rows`` without weights."""
     here = _device()
     tokens, row_bytes, px, top_k, pd, E, pc, po, pout = _permute_rows_args(here, x, dest, counts, expert_offsets, M, out)
     if out is None:
@@ -430,7 +436,8 @@ def check_combine_args(y, dest, weights=None, out=None):
 
 def bsgemm_combine_rows(y, dest, weights=None, out=None, stream=None):
     """Weighted sum of the rows of each token's picks: ``y`` [M, K] -> [tokens, K]. Without ``weights``
-    (float32 [tokens, top_k]) the plain sum, which is the gradient of ``bsgemm_permute_rows``."""
+    (float32 [tokens, top_k]) the plain sum, which is the gradient of ``bsgemm_permute_rows``. The result is detached
+    from autograd: the gradient is ``bsgemm_combine_backward``, without weights ``bsgemm_permute_rows``."""
     here = _device()
     M, K, code, tokens, py, top_k, pd, pw, po = _combine_args(here, y, dest, weights, out)
     if out is None:

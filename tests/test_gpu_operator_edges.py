@@ -245,3 +245,13 @@ def test_route_sort_work_grows_with_the_picks():
     short, long = best(1 << 18), best(1 << 21)
     say(f"[sort] 4096 experts: 2^18 picks {1e3 * short:.0f} us, 2^21 {1e3 * long:.0f} us")
     assert long <= 16 * short
+
+
+def test_results_are_detached():
+    """Inputs that require a gradient are taken as they are, and results carry no history, as documented."""
+    leaf = lambda *shape: torch.randn(*shape, device="cuda").requires_grad_()  # noqa: E731
+    dest, c, o, _, _ = bsg.bsgemm_route_sort(torch.tensor([[0, 1]] * 4, dtype=torch.int32, device="cuda"), 2, 4, 512)
+    results = [bsg.bsgemm_permute_rows(leaf(4, 64), dest, c, o, 512), bsg.bsgemm_combine_rows(leaf(512, 64), dest, leaf(4, 2)),
+               bsg.bsgemm_swiglu_backward(leaf(4, 64), leaf(4, 128)),
+               *bsg.bsgemm_rms_norm_quantize(leaf(4, 128), leaf(128), E4M3_BLOCK, residual=leaf(4, 128))[2:]]
+    assert not any(t.requires_grad for t in results)
